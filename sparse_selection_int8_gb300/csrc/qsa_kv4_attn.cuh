@@ -511,6 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_kv4_attn_kernel(const AttnPar
         ms.abort = 0;
         fence_mbar_init();
     }
+    // rows of the pool from the start: a wait that runs out lets the copies read them early
+    for (int i = tid; i < kRow * kTile; i += kThreads) (&ms.row[0][0])[i] = 0u;
     if (w == kSWarp) {
         tmem_alloc(&ms.tmem, kTmemCols);
         tmem_relinquish();

@@ -95,6 +95,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) qsa_kv4_wide_kernel(const Att
         ms.abort = 0;
         fence_mbar_init();
     }
+    // rows of the pool from the start: a wait that runs out lets the loads read them early
+    for (int i = tid; i < kWRow * kTile; i += kWideThreads) (&ms.row[0][0])[i] = 0u;
     if (w == kWMma) {
         tmem_alloc(&ms.tmem, 512);
         tmem_relinquish();

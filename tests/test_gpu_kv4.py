@@ -490,6 +490,35 @@ def test_attend_times_out_and_recovers(qsa, kw, t):
     call.check()
 
 
+TIMED = [(dict(lens=(600,)), "f32"), (dict(n_seq=6, G=2, T=4, lens=(2000, 100)), "f32"),
+         (dict(n_seq=20, G=2, H=8, lens=(2000,)), "bf16"), (dict(n_seq=9, G=2, T=3, lens=(1500, 80)), "bf16"),
+         (dict(H=12, T=100, lens=(4100,)), "bf16")]
+
+
+@pytest.mark.parametrize("kw,t", TIMED, ids=str)
+def test_attend_times_out_behind_other_kernels(qsa, kw, t):
+    """A call whose waits all run out reads rows of the pool alone, whatever other kernels left in shared memory:
+    a wide window's operands, small blocks' codes, scores of fp32 windows."""
+    before = [Call(qsa, Attend(seed=70 + i, q_dtype=u, **k), u) for i, (k, u) in enumerate(TIMED)]
+    call = Call(qsa, Attend(seed=39, q_dtype=t, **kw), t)
+    want = call().clone()
+    pool, scale = call.pool.clone(), call.scale.clone()
+    for other in before:
+        qsa.qsa_set_wait_limit(0)
+        other()
+        qsa.qsa_set_wait_limit(16)
+        try:
+            call()
+        finally:
+            qsa.qsa_set_wait_limit(0)
+        torch.cuda.synchronize()
+        assert int(call.status.item()) == qsa.QSA_STATUS_TIMEOUT
+        call.status.zero_()
+    assert torch.equal(call.pool, pool) and torch.equal(call.scale, scale)
+    call.out.fill_(3)
+    assert torch.equal(call(), want)
+
+
 @pytest.mark.parametrize("H", [1, 2, 12, 24, 32])
 @pytest.mark.parametrize("t", ["f32", "bf16"])
 def test_attend_long_sums(qsa, H, t):
