@@ -418,9 +418,11 @@ struct Misc {
     int32_t lim[kMaxRows];
     int32_t odd[kMaxRows]; // the row's query is not finite
     float isg_max[2];      // largest 2^14 / sigma of a set's rows
-    long long off[kMaxRows]; // the rows' element offsets in q and out
+    // the rows' element offsets in q and out, by the segment's parity: a warp may stage
+    // a segment's queries while a slower one still stores the outputs of the one before
+    long long off[2][kMaxRows];
     float red[2][2][4][kMaxRows / 2]; // [set][what][warp][row] reductions
-    float delta[kMaxRows], fac[kMaxRows], ofac[kMaxRows], fin[kMaxRows], zsum[kMaxRows], lsum[kMaxRows];
+    float delta[kMaxRows], fac[kMaxRows], ofac[kMaxRows], fin[kMaxRows], zsum[kMaxRows];
     Walk first;
     long long total;
     uint32_t tmem;
@@ -758,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_kv4_attn_kernel(const AttnPar
                     (r & 1 ? d.nref.y : d.nref.x) = 0.f;
                     (r & 1 ? d.isg.y : d.isg.x) = r < n_rows ? kFresh : 0.f;
                     ms.lim[r] = lim_r;
-                    ms.off[r] = at_r;
+                    ms.off[seg & 1][r] = at_r;
                     ms.odd[r] = e == 255u;
                     if (r < 2) ms.isg_max[r] = r * RS < n_rows ? kFresh : 0.f;
                 }
@@ -1078,7 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_kv4_attn_kernel(const AttnPar
                     if (c0 + r >= n_rows) break;
                     const float o = fmaf(v[r], ms.fin[c0 + r], ms.zsum[c0 + r]);
                     if (direct) {
-                        const long long at = ms.off[c0 + r] + dim;
+                        const long long at = ms.off[seg & 1][c0 + r] + dim;
                         if (p.out_bf16) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16(o);
                         else static_cast<float *>(p.out)[at] = o;
                     } else {

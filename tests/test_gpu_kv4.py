@@ -307,6 +307,20 @@ def test_attend_repeats_bitwise_and_on_a_stream(qsa):
         assert torch.equal(call.out, first)
 
 
+@pytest.mark.parametrize("kw", [dict(n_seq=300, G=2, H=4, lens=(100, 1, 129, 40, 0, 128)), dict(n_seq=30, G=16, H=12, T=2, lens=(60, 200)),
+                                dict(n_seq=700, G=1, H=1, lens=(3, 90), dense=True, P=8, shared=True)], ids=str)
+@pytest.mark.parametrize("q,o", DTYPES)
+def test_attend_whole_pairs_in_a_row(qsa, kw, q, o):
+    """Several short (sequence, KV head) pairs to a multiprocessor, each written to its own place, time after time."""
+    call = Call(qsa, Attend(seed=71, q_dtype=q, **kw), o)
+    call.check()
+    first = call.out.clone()
+    for _ in range(40):
+        call.out.fill_(9)
+        call()
+        assert torch.equal(call.out, first)
+
+
 def test_attend_captured(qsa):
     """One graph serves other lengths within the bound: lists, limits and tables are read at replay."""
     a = Attend(seed=21, n_seq=4, G=2, lens=(700, 20, 300, 1), P=8, dense=True, causal=True)
