@@ -437,8 +437,9 @@ qsa_status qsa_kv4_read(const qsa_shape *shape, int32_t n_seq, int32_t n_pools, 
  * queries to 2^-22 of their value (bf16 ones exactly) or 2^-35 of their row's
  * largest, probabilities to 2^-22 (2^-11 where queries and output are bf16).
  * Unlike the other attention calls this one waits for the kernel before it, if
- * that let it start early, before it reads q: the output of one call may be the
- * query of the next.  Cells that a row does not see do not reach it, whatever
+ * that let it start early, before it reads any input: whatever that kernel
+ * writes may be one, and the output of one call may be the query of the next.
+ * (So do qsa_kv4_append, qsa_kv4_read and qsa_page_map.)  Cells that a row does not see do not reach it, whatever
  * their stored values; rows that do see a value that is not finite, or whose
  * query holds one, are not finite, and no other row is.  Two
  * launches; allocates nothing, graph-capturable.  Errors: QSA_ERR_INVALID_ARG;

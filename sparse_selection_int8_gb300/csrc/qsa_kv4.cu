@@ -43,13 +43,13 @@ struct Row8 {
     __device__ __forceinline__ void load(const void *base, size_t row, int lane)
     {
         if constexpr (BF16) {
-            const uint4 a = ldg_nc_v4(static_cast<const uint8_t *>(base) + row * kHeadDim * 2 + 16 * lane);
+            const uint4 a = load_late(static_cast<const uint4 *>(base) + row * (kHeadDim / 8) + lane);
             w[0] = a.x;
             w[1] = a.y;
             w[2] = a.z;
             w[3] = a.w;
         } else {
-            sm100::ldg256_stream(static_cast<const uint8_t *>(base) + row * kHeadDim * 4 + 32 * lane, w);
+            load_late256(static_cast<const uint8_t *>(base) + row * kHeadDim * 4 + 32 * lane, w);
         }
     }
 
@@ -199,9 +199,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kKv4Blocks) qsa_kv4_append_ker
 {
     const int lane = threadIdx.x & 31;
     const uint32_t stride = gridDim.x * kKv4Warps;
-    // (Launched early behind a kernel that allows it, and lets none follow before its
-    // end: the attention reads the cells at once.  Reads of what that kernel may write are plain
-    // or volatile ones, which stay behind the wait.)
+    // (Launched early behind a kernel that allows it; whatever that kernel wrote is read
+    // behind the wait, by loads that stay there.)
     cudaGridDependencySynchronize();
     uint32_t i = blockIdx.x * kKv4Warps + (threadIdx.x >> 5);
     Row8<BF16> k, v;
@@ -234,7 +233,6 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kKv4Blocks) qsa_kv4_append_ker
         v = vn;
         i = next;
     }
-    __threadfence(); // an attention launched behind this reads the cells ahead of its wait
 }
 
 // The lane's 8 values of a word of codes.

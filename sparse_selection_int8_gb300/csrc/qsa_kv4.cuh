@@ -49,14 +49,22 @@ __device__ __forceinline__ int kv4_resolve(const Kv4Pool &p, int b, int pos, uin
     return kv4_slot(p, p.page_table[(size_t)b * p.page_table_len + page], pos - page * P, bad);
 }
 
-// A load that stays behind cudaGridDependencySynchronize(), of data that the
-// kernel before may have written (no read-only path, no L1).
+// Loads that stay behind cudaGridDependencySynchronize(), of data that the kernel
+// before may have written while this one was being launched (no read-only path, no
+// L1).
 __device__ __forceinline__ uint4 load_late(const uint4 *ptr)
 {
     uint4 v;
     asm volatile("ld.global.cg.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(ptr) : "memory");
     return v;
+}
+
+__device__ __forceinline__ void load_late256(const void *ptr, uint32_t *r) // 32-byte aligned
+{
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(ptr) : "memory");
 }
 
 // Two fp32 values in one operation.

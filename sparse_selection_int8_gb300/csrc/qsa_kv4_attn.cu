@@ -59,21 +59,22 @@ __global__ void __launch_bounds__(kMergeWarps * 32) qsa_kv4_merge_kernel(const A
     __shared__ float s_part[W > 1 ? kMergeWarps : 1][kHeadDim];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long row = W > 1 ? blockIdx.x : (long long)blockIdx.x * kMergeWarps + warp;
-    // the next call may launch: it writes nothing before this grid is done
+    // the next call may launch: it reads and writes nothing before this grid is done
     cudaTriggerProgrammaticLaunchCompletion();
     if (row >= rows) return; // (with W > 1 the grid has a CTA per row)
     const int bg = (int)(row / p.R), r = (int)(row - (long long)bg * p.R);
     const int b = bg / p.pool.G, g = bg - b * p.pool.G, rb = r / p.rb_rows;
     const int local = r - rb * p.rb_rows;
-    int start, n;
-    list_of(p, b, start, n);
     const size_t out_at = row_offset(p, b, g, r);
     cudaGridDependencySynchronize();
+    // (the list's range and the pair's parts in one go: without cells the latter mean nothing)
+    const int2 info = p.max_selected > 0 ? p.info[(long long)bg * p.n_rb + rb] : make_int2(0, 0);
+    int start, n;
+    list_of(p, b, start, n);
     float o[8], L = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = 0.f;
     if (n > 0) {
-        const int2 info = p.info[(long long)bg * p.n_rb + rb];
         if (info.y == 1) return;
         auto slot = [&](int i) { return (size_t)(i == 0 ? info.x : 2 * ((info.x >> 1) + i)) * p.slot_rows + local; };
         auto part = [&](int i, float4 &x, float4 &y) {

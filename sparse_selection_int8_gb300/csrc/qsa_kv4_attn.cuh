@@ -61,11 +61,12 @@ __device__ __forceinline__ void raise(const AttnParams &p, uint32_t bits)
     if (bits && p.status) atomicOr(p.status, bits);
 }
 
-// List range of sequence b (bad offsets are clamped).
+// List range of sequence b (bad offsets are clamped).  (Here and below: plain loads,
+// of what the kernel before may have written.)
 __device__ __forceinline__ uint32_t list_of(const AttnParams &p, int b, int &start, int &n)
 {
-    start = __ldg(p.sel_offsets + b);
-    const long long len = (long long)__ldg(p.sel_offsets + b + 1) - start;
+    start = p.sel_offsets[b];
+    const long long len = (long long)p.sel_offsets[b + 1] - start;
     if (start < 0 || len < 0) {
         start = n = 0;
         return QSA_STATUS_BAD_OFFSETS;
@@ -519,6 +520,11 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_kv4_attn_kernel(const AttnPar
         tmem_alloc(&ms.tmem, kTmemCols);
         tmem_relinquish();
     }
+    // All input is read behind this: the kernel before may have written any of it (the
+    // merge of a call whose output is this one's query, a copy into a list or a page
+    // table), and its writes are promised here only; it may also still read the
+    // partials that this one writes.
+    cudaGridDependencySynchronize();
     if (w == kSoft0) {
         Walk f;
         long long t;
@@ -655,9 +661,6 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_kv4_attn_kernel(const AttnPar
         const uint32_t t_lane = (uint32_t)(32 * q) << 16;
         Walk it = ms.first;
         const long long total = ms.total;
-        // The kernel before may be the merge of a call whose output is this one's
-        // query, and may still read the partials that this one writes.
-        cudaGridDependencySynchronize();
         uint32_t i = 0; // tile
         uint32_t seg = 0;
         float2 l[RS / 2], z[RS / 2]; // this thread's sums of p and of p vz, by row
@@ -671,8 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_kv4_attn_kernel(const AttnPar
             // in [2^14, 2^15), as f16 parts (rows of the B operand), in the order of
             // the K codes; a warp per row, lane = word of codes.
             if (seg > 0) wait(&ms.q_empty, seg - 1);
-            // (a rolled loop, the next row loaded ahead: this code runs cold; loads by
-            // L2, since the rows may have been written after this kernel's launch)
+            // (a rolled loop, the next row loaded ahead: this code runs cold)
             uint4 raw[PARTS];
             int lim = -1;
             long long at = 0;
@@ -1223,7 +1225,7 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_kv4_attn_kernel(const AttnPar
                     if (c_in[k]) {
                         const int page = p.page_shift >= 0 ? a_pos[k] >> p.page_shift : a_pos[k] / p.pool.page_cells;
                         c_off[k] = a_pos[k] - page * p.pool.page_cells;
-                        c_entry[k] = __ldg(p.pool.page_table + (size_t)a_b * p.pool.page_table_len + page);
+                        c_entry[k] = p.pool.page_table[(size_t)a_b * p.pool.page_table_len + page];
                     }
                     a_in[k] = false;
                 }
@@ -1235,7 +1237,7 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_kv4_attn_kernel(const AttnPar
                     for (int k = 0; k < 2; ++k) {
                         const int i = i0 + 32 * k;
                         a_in[k] = i < head.n;
-                        if (a_in[k]) a_pos[k] = p.sel ? __ldg(p.sel + head.start + i) : i;
+                        if (a_in[k]) a_pos[k] = p.sel ? p.sel[(long long)head.start + i] : i;
                     }
                     walk_next(p, head, 1);
                 }
@@ -1246,8 +1248,6 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_kv4_attn_kernel(const AttnPar
     __syncthreads();
     tc_fence_after();
     if (w == kSWarp) tmem_dealloc(tmem, kTmemCols);
-    // (a CTA without work too: this grid does not end before the one before it)
-    cudaGridDependencySynchronize();
 }
 
 template <int RS, int PARTS>

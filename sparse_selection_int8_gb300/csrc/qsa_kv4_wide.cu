@@ -101,6 +101,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) qsa_kv4_wide_kernel(const Att
         tmem_alloc(&ms.tmem, 512);
         tmem_relinquish();
     }
+    // All input is read behind this (see qsa_kv4_attn_kernel).
+    cudaGridDependencySynchronize();
     if (w == 0) {
         Walk f;
         long long t;
@@ -145,9 +147,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) qsa_kv4_wide_kernel(const Att
         const uint32_t pair_bar = 1 + (w & 3); // the warps of the two halves
         Walk it = ms.first;
         const long long total = ms.total;
-        // The kernel before may be the merge of a call whose output is this one's
-        // query, and may still read the partials that this one writes.
-        cudaGridDependencySynchronize();
         uint32_t i = 0; // tile
 #pragma unroll 1
         for (uint32_t seg = 0; it.left > 0; ++seg) {
@@ -158,7 +157,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) qsa_kv4_wide_kernel(const Att
             // A warp per row, lane = eight dimensions: scaled by a power of two so
             // that the row's largest magnitude lies in [2^14, 2^15), in the order of
             // the codes (dimensions 0 4 1 5 2 6 3 7, the odd ones' codes counting 16
-            // times).  (Loads by L2: the rows may be younger than this launch.)
+            // times).
 #pragma unroll 1
             for (int r0 = w; r0 < kTile; r0 += 4 * kWSoft) {
                 uint4 raw[4]; // four rows in flight
@@ -519,7 +518,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) qsa_kv4_wide_kernel(const Att
             const uint8_t *src = p.codes + (size_t)ms.row[e][cell] * QSA_KV4_CODE_BYTES + (is_v ? 128 : 0);
             mbar_arrive(&ms.row_empty[e]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) ldg256_stream(src + 32 * c, raw + 8 * c);
+            for (int c = 0; c < 4; ++c) load_late256(src + 32 * c, raw + 8 * c);
         };
         if (tiles > 0) fetch(0);
 #pragma unroll 1
@@ -660,7 +659,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) qsa_kv4_wide_kernel(const Att
                         const uint32_t r = (uint32_t)(base + max(slot, 0));
                         ms.row[e][c0 + 32 * k] = r;
                         d_pos[k] = slot >= 0 ? c_pos[k] : 0x7fffffff;
-                        f[k] = slot >= 0 ? __ldg(p.scale + r) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        f[k] = slot >= 0 ? p.scale[r] : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
                     raise(p, bad & ~QSA_STATUS_NOT_RESIDENT);
                     mbar_arrive(&ms.row_full[e]);
@@ -678,7 +677,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) qsa_kv4_wide_kernel(const Att
                     if (c_in[k]) {
                         const int page = p.page_shift >= 0 ? a_pos[k] >> p.page_shift : a_pos[k] / p.pool.page_cells;
                         c_off[k] = a_pos[k] - page * p.pool.page_cells;
-                        c_entry[k] = __ldg(p.pool.page_table + (size_t)a_b * p.pool.page_table_len + page);
+                        c_entry[k] = p.pool.page_table[(size_t)a_b * p.pool.page_table_len + page];
                     }
                     a_in[k] = false;
                 }
@@ -690,7 +689,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) qsa_kv4_wide_kernel(const Att
                     for (int k = 0; k < 2; ++k) {
                         const int i = i0 + 32 * k;
                         a_in[k] = i < head.n;
-                        if (a_in[k]) a_pos[k] = p.sel ? __ldg(p.sel + head.start + i) : i;
+                        if (a_in[k]) a_pos[k] = p.sel ? p.sel[(long long)head.start + i] : i;
                     }
                     walk_next(p, head, 1);
                 }
@@ -701,8 +700,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) qsa_kv4_wide_kernel(const Att
     __syncthreads();
     tc_fence_after();
     if (w == kWMma) tmem_dealloc(tmem, 512);
-    // (a CTA without work too: this grid does not end before the one before it)
-    cudaGridDependencySynchronize();
 }
 
 } // namespace

@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(T) qsa_page_map_kernel(const PageParams p, int
         const int b = t / p.max_new, cur = held_before(p, b);
         map_tokens<1>(p, b, t - b * p.max_new, cur, p.out_len[b] - cur);
     }
-    __threadfence(); // an attention launched behind this reads tables and offsets ahead of its wait
+    __threadfence(); // an INT8 attention launched behind this reads tables and offsets ahead of its wait
 }
 
 // A block row per sequence; W tokens per thread (16-byte stores where the rows

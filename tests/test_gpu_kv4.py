@@ -475,6 +475,73 @@ def test_attend_output_is_the_next_query(qsa, t, kw):
         check()
 
 
+@pytest.mark.parametrize("what", ["table", "sel", "offsets", "limit"])
+@pytest.mark.parametrize("kw,t", [(dict(H=12, lens=(300,)), "f32"), (dict(H=12, T=100, lens=(4100,)), "bf16")], ids=str)
+def test_attend_output_is_another_input_of_the_next(qsa, what, kw, t):
+    """A call whose rows see nothing writes zeros over the table, list, offsets or limits that the next call,
+    launched right behind it, reads."""
+    first = Attend(seed=72, H=20, lens=(12800,), P=64, dense=True, causal=True)
+    first.q_limit[:] = 0
+    c = Attend(seed=73, q_dtype=t, causal=True, context=5000, **kw)
+    name = dict(table="page_table", sel="sel", offsets="offsets", limit="q_limit")[what]
+    old = getattr(c, name)
+    a, b = Call(qsa, first, "f32"), Call(qsa, c, t)
+    assert old.size <= a.out.numel()
+    a.out = torch.empty(a.out.numel(), dtype=torch.int32, device="cuda")
+    buf = a.out[:old.size].view(old.shape)
+    setattr(b, what, buf)
+    setattr(c, name, np.zeros_like(old))
+    data = dev(old)
+    b.out.fill_(3)
+    for _ in range(10):
+        buf.copy_(data)
+        a()
+        b.check(what)
+
+
+@pytest.mark.parametrize("kw,t", [(dict(lens=(600,)), "f32"), (dict(n_seq=16, G=2, T=4, lens=(2000, 100, 700)), "bf16"),
+                                  (dict(H=12, T=100, lens=(4100,)), "bf16")], ids=str)
+def test_attend_behind_ordinary_kernels(qsa, kw, t):
+    """Each input in turn written by a framework's kernel right before the call."""
+    calls = [Call(qsa, Attend(seed=74 + i, q_dtype=t, P=4, causal=True, context=4500, **kw), t) for i in range(2)]
+    want = [c().clone() for c in calls]
+    torch.cuda.synchronize()
+    names = ["sel", "offsets", "table", "limit", "q", "scale", "pool"]
+    got = Call(qsa, calls[0].c, t)
+    for last in range(len(names)):
+        for i in range(12):
+            for n in names[last + 1:] + names[:last + 1]:
+                torch.add(getattr(calls[i & 1], n), 0, out=getattr(got, n))
+            got()
+            assert torch.equal(got.out, want[i & 1]), names[last]
+
+
+def test_attend_behind_the_append_at_once(qsa):
+    """Cells appended right before they are attended to, over and over into the same slots."""
+    c = Attend(seed=76, lens=(256,), P=1, dense=True)
+    call = Call(qsa, c, "f32")
+    rng = np.random.default_rng(77)
+    pos = dev(np.arange(256, dtype=np.int32)[None])
+    rows = [[dev(rng.standard_normal((1, 256, 1, 256)).astype(np.float32)) for _ in "kv"] for _ in range(2)]
+
+    def step(i):
+        qsa.qsa_kv4_append(call.shape, 1, 1, 256, qsa.QSA_F32, *rows[i], pos, call.table, call.pool, call.scale)
+    want = []
+    for i in range(2):
+        step(i)
+        torch.cuda.synchronize()
+        want.append(call().clone())
+        torch.cuda.synchronize()
+    assert not torch.equal(*want)
+    outs = [torch.empty_like(call.out) for _ in range(60)]
+    for i, o in enumerate(outs):
+        step(i & 1)
+        call.out = o
+        call()
+    for i, o in enumerate(outs):
+        assert torch.equal(o, want[i & 1])
+
+
 def test_attend_fewer_cells_than_the_workspace_was_sized_for(qsa):
     """A workspace of the largest bound serves every smaller one."""
     big = Attend(seed=36, n_seq=3, T=4, lens=(4000,))
