@@ -366,7 +366,9 @@ __global__ void __launch_bounds__(256) qsa_token_map_kernel(const PageParams p)
 {
     cudaGridDependencySynchronize(); // lengths and tables
     const int b = blockIdx.y, cur = held_before(p, b), n = p.out_len[b] - cur;
-    for (int i = (blockIdx.x * 256 + threadIdx.x) * W; i < p.max_new; i += gridDim.x * 256 * W) map_tokens<W>(p, b, i, cur, n);
+    // (unsigned: the step past the last token may exceed 2^31, not 2^32)
+    for (uint32_t i = (blockIdx.x * 256 + threadIdx.x) * W; i < (uint32_t)p.max_new; i += gridDim.x * 256 * W)
+        map_tokens<W>(p, b, (int)i, cur, n);
     // (no fence: what this writes, positions, slots and limits, is read behind waits alone)
 }
 

@@ -758,6 +758,32 @@ def test_page_map_roll_back_and_grow(qsa, shared):
     assert not state["status"].any()
 
 
+@pytest.mark.parametrize("max_new", [2 ** 31 - 1, 2 ** 31 - 4, 2 ** 31 - 2 ** 20 + 3])
+def test_page_map_widest_maps(qsa, max_new):
+    """Maps near the largest width: the stride behind the last token passes 2^31."""
+    P, L, cur, new = 64, 1 << 22, 5, 200_000_007
+    table = torch.full((1, L), -1, dtype=torch.int32, device="cuda")
+    table[0, 0] = 0
+    pages = L
+    free = torch.arange(pages - 1, -1, -1, dtype=torch.int32, device="cuda")[None].contiguous()
+    count = dev(np.array([pages - 1], np.int32))
+    out_len, offsets, status = (torch.full((k,), v, dtype=torch.int32, device="cuda") for k, v in ((1, 7), (2, 7), (1, 0)))
+    guard = 4096
+    maps = [torch.full((max_new + guard,), 77, dtype=torch.int32, device="cuda") for _ in range(3)]
+    qsa.qsa_page_map(1, 1, max_new, P, L, pages, dev(np.array([cur], np.int32)), dev(np.array([new], np.int32)), table, free,
+                     count, out_len, offsets, *maps, status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and int(out_len.item()) == new
+    n = new - cur
+    want = torch.arange(cur, new, dtype=torch.int32, device="cuda")
+    assert torch.equal(maps[0][:n], want) and torch.equal(maps[2][:n], want + 1)
+    assert torch.equal(maps[1][:n], want)  # pages taken in order: 1, 2, ...
+    for m, fill in zip(maps, (-1, -1, 0)):
+        for part in m[n:max_new].split(1 << 28):
+            assert bool((part == fill).all())
+        assert bool((m[max_new:] == 77).all())
+
+
 @pytest.mark.parametrize("max_new", [8, 300])
 def test_page_map_then_attention_at_once(qsa, max_new):
     """The attention launched right behind the page map reads the tables and offsets that it has written."""
