@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) qsa_kv_append_kernel(const 
             if (g + 1 < p.G) store_item<BF16>(p, k1, v1, cell0 + (size_t)(g + 1) * p.pool_cells, lane);
         }
     }
+    __threadfence(); // an attention launched behind this reads the pools ahead of its wait
 }
 
 bool aligned(const void *ptr, size_t a) { return ((uintptr_t)ptr % a) == 0; }

@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(256) qsa_token_map_kernel(const PageParams p)
     // (unsigned: the step past the last token may exceed 2^31, not 2^32)
     for (uint32_t i = (blockIdx.x * 256 + threadIdx.x) * W; i < (uint32_t)p.max_new; i += gridDim.x * 256 * W)
         map_tokens<W>(p, b, (int)i, cur, n);
-    // (no fence: what this writes, positions, slots and limits, is read behind waits alone)
+    __threadfence(); // (the limits: as for the tables)
 }
 
 } // namespace

@@ -391,6 +391,7 @@ __global__ void __launch_bounds__(256) qsa_select_expand_kernel(const SelParams 
         for (int i = lane; i < cells; i += 32) p.sel[base + i] = start + i;
         base += cells;
     }
+    __threadfence(); // an INT8 attention launched behind this reads the list ahead of its wait
 }
 
 struct SelWorkspace {
