@@ -106,7 +106,7 @@ def test_limited_attention_behind_the_page_map(qsa, T):
     count = torch.full((B,), L, **i32)
     out_len, offsets = torch.zeros(B, **i32), torch.zeros(B + 1, **i32)
     positions, slots, limit = (torch.zeros((B, T), **i32) for _ in range(3))
-    first = [0, 3 * T // 4]  # each set's first position
+    first = [0, T // 4]  # each set's first position
     length = {x: torch.full((B,), x, **i32) for f in first for x in (f, f + T)}
     held = [0]
 
