@@ -799,11 +799,9 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_kv4_attn_kernel(const AttnPar
                 // a cell that no row sees counts nothing, whatever it holds
                 const bool none = pos >= lim_max;
                 if (none) f = make_float4(0.f, 0.f, 0.f, 0.f);
-                // limits between the rows: row by row, and with care where an
-                // unseen cell's V scale or zero is not finite
+                // limits between the rows: row by row
                 const bool by_row = lim_min < 0 || __any_sync(0xffffffffu, !none && pos >= lim_min);
                 f.w = fmaf(7.5f, f.z, f.w); // (V's codes go in less 7.5)
-                const bool care = by_row && __any_sync(0xffffffffu, !(fabsf(f.z) < INFINITY && fabsf(f.w) < INFINITY));
                 const float avs = none ? 0.f : fmaxf(fabsf(f.z), 0x1p-98f);
                 const float2 ks = make_float2(f.x, f.x), kz = make_float2(f.y, f.y), vs = make_float2(f.z, f.z),
                              vz = make_float2(f.w, f.w);
@@ -963,10 +961,12 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_kv4_attn_kernel(const AttnPar
                         const float2 pe2 = make_float2(fast_exp2(x[r].x), fast_exp2(x[r].y));
                         float2 pv;
                         l[r] = add2(l[r], pe2);
-                        if (!care) {
+                        if (!by_row) {
                             z[r] = fma2(pe2, vz, z[r]);
                             pv = mul2(pe2, mul2(vs, isg));
-                        } else { // (what an unseen cell holds must not reach the row)
+                        } else {
+                            // what an unseen cell holds must not reach the row: not finite, or
+                            // finite but beyond the row's sigma, which may be far below it
                             float2 &zr = z[r];
                             pv.x = x[r].x != -INFINITY ? pe2.x * (f.z * isg.x) : 0.f;
                             pv.y = x[r].y != -INFINITY ? pe2.y * (f.z * isg.y) : 0.f;

@@ -40,7 +40,6 @@ struct WideMisc {
     int32_t pos[kWPrm][kTile];   // 2^31 - 1 where there is no cell
     int32_t pos_max[kWPrm][2];   // of a lookup warp's 64 cells
     float vs_max[kWPrm][2];      // largest |vs| of them
-    int32_t odd[kWPrm][2];       // a V scale or zero among them is not finite
     uint32_t row[kWRow][kTile];  // the cells' rows in the pool
     float2 score[kTile];         // the rows' scales and sum(q)
     float2 fin[kTile];           // what their sums are scaled by and get added in the end
@@ -234,7 +233,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) qsa_kv4_wide_kernel(const Att
                 wait(&ms.prm_full[pe], i / kWPrm);
                 // cells that some row of the warp does not see: row by row
                 const bool by_row = max(ms.pos_max[pe][0], ms.pos_max[pe][1]) >= lim_min;
-                const bool care = by_row && (ms.odd[pe][0] | ms.odd[pe][1]);
                 const float v_all = fmaxf(ms.vs_max[pe][0], ms.vs_max[pe][1]);
                 wait(&ms.s_full[par], i >> 1);
                 tc_fence_after();
@@ -391,7 +389,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) qsa_kv4_wide_kernel(const Att
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             float2 vs = make_float2(f.x, f.y), vz = make_float2(f.z, f.w);
-                            if (care) { // (what an unseen cell holds must not reach the row)
+                            if (by_row) { // (what an unseen cell holds must not reach the row, finite or not)
                                 if (t[j][k].x == -INFINITY) vs.x = vz.x = 0.f;
                                 if (t[j][k].y == -INFINITY) vs.y = vz.y = 0.f;
                             }
@@ -617,11 +615,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) qsa_kv4_wide_kernel(const Att
                     if (j >= kWPrm) wait(&ms.prm_empty[e], j / kWPrm - 1);
                     int top = -1;
                     float v = 0.f;
-                    bool odd = false;
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int c = c0 + 32 * k;
-                    f[k].w = fmaf(7.5f, f[k].z, f[k].w); // (V's codes go in less 7.5)
+                        f[k].w = fmaf(7.5f, f[k].z, f[k].w); // (V's codes go in less 7.5)
                         float *const kp = &ms.k[e][c >> 1].x + (c & 1), *const vp = &ms.v[e][c >> 1].x + (c & 1);
                         kp[0] = f[k].x;
                         kp[2] = f[k].y;
@@ -630,15 +627,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) qsa_kv4_wide_kernel(const Att
                         ms.pos[e][c] = d_pos[k];
                         top = max(top, d_pos[k]);
                         v = fmaxf(v, fabsf(f[k].z));
-                        odd |= !(fabsf(f[k].z) < INFINITY && fabsf(f[k].w) < INFINITY);
                     }
                     top = __reduce_max_sync(0xffffffffu, top);
                     v = warp_max(v);
-                    odd = __any_sync(0xffffffffu, odd);
                     if (lane == 0) {
                         ms.pos_max[e][half] = top;
                         ms.vs_max[e][half] = v;
-                        ms.odd[e][half] = odd;
                     }
                     mbar_arrive(&ms.prm_full[e]);
                 }

@@ -267,6 +267,45 @@ def test_attend_limits_in_any_order(qsa):
     assert np.linalg.norm(got[0, 2:] - clean[0, 2:]) <= 2e-5 * np.linalg.norm(clean[0, 2:])
 
 
+@pytest.mark.parametrize("big", [2.0 ** 14, 2.0 ** 20, 2.0 ** 60, 2.0 ** 100])
+@pytest.mark.parametrize("kw,q,o", [(dict(lens=(300,), T=4), "f32", "f32"), (dict(lens=(300,), T=4), "bf16", "bf16"),
+                                    (dict(lens=(3000,), T=4, G=2), "f32", "f32"), (dict(lens=(3000,), T=4, H=3), "bf16", "bf16"),
+                                    (dict(n_seq=40, lens=(500, 90), T=4, G=2, H=4), "bf16", "f32"),
+                                    (dict(lens=(4097,), T=100), "bf16", "bf16")], ids=str)
+def test_attend_unseen_scales_of_any_size(qsa, big, kw, q, o):
+    """Finite V scales that a row does not see do not reach it, in pairs of one part and of several, also
+    where the row has seen no cell yet; padding rows (limit 0) are zeros."""
+    c = Attend(seed=80, P=4, dense=True, causal=True, q_dtype=q, **kw)
+    n = int(c.offsets[1])
+    c.kv_scale[..., 2:] *= np.float32(big ** -0.5)
+    c.q_limit[:, :] = np.linspace(0, n // 3, c.T).astype(int)
+    c.q_limit[:, -1] = n
+    for b in range(c.n_seq):
+        pos = np.arange(n // 3, c.context)
+        e = c.page_table[b, pos // 4]
+        c.kv_scale[b, :, e * 4 + pos % 4, 2:] *= np.float32(big ** 0.75)
+        c.kv_scale[b, :, e * 4 + pos % 4, 2:] *= np.float32(big ** 0.75)
+    Call(qsa, c, o).check()
+
+
+@pytest.mark.parametrize("kw,t", [(dict(lens=(300, 77), n_seq=2, holes=0.1, T=2), "f32"), (dict(lens=(3001,), G=2, holes=0.1), "bf16"),
+                                  (dict(lens=(700,), T=3, dense=True, causal=True), "f32"),
+                                  (dict(lens=(4100,), T=100, holes=0.05), "bf16"),
+                                  (dict(lens=(4097,), T=100, dense=True, causal=True), "bf16")], ids=str)
+@pytest.mark.parametrize("scale", [0.0, -0.0, -1.0 / 16, 2.0 ** -30, -(2.0 ** -60), 2.0 ** -120])
+def test_attend_softmax_scales(qsa, scale, kw, t):
+    """No scale (the mean of the values), negative and tiny ones, with masked pages and lists that end inside a tile."""
+    c = Attend(seed=81, P=4, q_dtype=t, **kw)
+    c.softmax_scale = scale
+    Call(qsa, c, t).check()
+    c.q[0, 0, 0] = 0  # a row of zeros
+    Call(qsa, c, t).check("zeros")
+    if abs(scale) < 1e-3:
+        c.kv_scale[..., :2] *= np.float32(2.0 ** 118)  # scores stay small beside the scale
+        c.q *= np.float32(2.0 ** -100)
+        Call(qsa, c, t).check("K scales")
+
+
 def test_attend_nonfinite_queries_stay_in_their_row(qsa):
     c = Attend(seed=17, lens=(300,), T=2)
     clean = c.reference()[0]
