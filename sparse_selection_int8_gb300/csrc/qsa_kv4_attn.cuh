@@ -81,6 +81,16 @@ __device__ __forceinline__ int query_of(const AttnParams &p, int r)
     return p.H == 1 ? r : (int)__umulhi((uint32_t)r, p.h_mul);
 }
 
+// What a row's sums from the tensor cores (of codes u 2^-24 and queries scaled up from
+// exponent e) are multiplied by to be scores in log2 units: 2^(e - 141) 2^24 |scale|, in
+// an order that neither over- nor underflows before the result does.  Where that
+// underflows (a softmax scale of 0, say) it is the smallest positive number, so that a masked
+// cell's -inf stays -inf; all other scores vanish (the sums are below 2^127).
+__device__ __forceinline__ float row_scale(const AttnParams &p, uint32_t e)
+{
+    return fmaxf(__uint_as_float((e - 2u) << 23) * (fabsf(p.scale_log2) * 0x1p12f), 0x1p-149f);
+}
+
 // Element offset of row r of (sequence b, KV head g) in q and out.
 __device__ __forceinline__ size_t row_offset(const AttnParams &p, int b, int g, int r)
 {
@@ -719,7 +729,6 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_kv4_attn_kernel(const AttnPar
                 for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(x[k]) & 0x7fffffffu);
                 const uint32_t e = max(__reduce_max_sync(0xffffffffu, top) >> 23, 15u);
                 float up = __uint_as_float((268u - min(e, 254u)) << 23);
-                const float down = __uint_as_float((e - 14u) << 23);
                 if (p.scale_log2 < 0.f) up = -up; // (the scale below is positive)
                 float sum = 0.f;
 #pragma unroll
@@ -752,11 +761,11 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_kv4_attn_kernel(const AttnPar
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 if (lane == 0) {
-                    // the MMA's codes are u 2^-24: scores come out of it, and sum(q)
-                    // goes in, 2^24 too small; a row that is not finite has no scores
+                    // (sum(q) goes in 2^24 too small, as the scores come out of the MMA; a
+                    // row that is not finite has no scores)
                     RowScore &c = ms.score[r >> 1];
                     RowRef &d = ms.ref[r >> 1];
-                    const float xs = e < 255u ? down * fabsf(p.scale_log2) * 0x1p24f : __uint_as_float(0x7fffffffu);
+                    const float xs = e < 255u ? row_scale(p, e) : __uint_as_float(0x7fffffffu);
                     (r & 1 ? c.xs.y : c.xs.x) = xs;
                     (r & 1 ? c.qz.y : c.qz.x) = sum * 0x1p-24f;
                     (r & 1 ? d.nref.y : d.nref.x) = 0.f;

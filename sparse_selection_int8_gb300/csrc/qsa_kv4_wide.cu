@@ -185,7 +185,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) qsa_kv4_wide_kernel(const Att
                     }
                     const uint32_t e = max(__reduce_max_sync(0xffffffffu, top) >> 23, 15u);
                     float up = __uint_as_float((268u - min(e, 254u)) << 23);
-                    const float down = __uint_as_float((e - 14u) << 23);
                     if (p.scale_log2 < 0.f) up = -up; // (the scale below is positive)
 #pragma unroll
                     for (int k = 0; k < 8; ++k) x[k] *= up;
@@ -202,12 +201,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) qsa_kv4_wide_kernel(const Att
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     if (lane == 0) {
-                        // the MMA's codes are u 2^-24: scores come out of it, and sum(q)
-                        // goes in, 2^24 too small.  A row that is not finite has NaN for
-                        // the scores that it sees; a scale of 0 stays above it, so that
-                        // it leaves -inf as it is.
-                        const float xs = down * fabsf(p.scale_log2) * 0x1p24f;
-                        ms.score[r] = make_float2(e == 255u ? 1.f : xs == 0.f ? 0x1p-126f : xs,
+                        // (sum(q) goes in 2^24 too small, as the scores come out of the
+                        // MMA; a row that is not finite has NaN for the scores that it sees)
+                        ms.score[r] = make_float2(e == 255u ? 1.f : row_scale(p, e),
                                                   e == 255u ? __uint_as_float(0x7fffffffu) : sum * 0x1p-24f);
                         ms.lim[r] = lim;
                     }

@@ -301,8 +301,8 @@ def test_attend_softmax_scales(qsa, scale, kw, t):
     c.q[0, 0, 0] = 0  # a row of zeros
     Call(qsa, c, t).check("zeros")
     if abs(scale) < 1e-3:
-        c.kv_scale[..., :2] *= np.float32(2.0 ** 118)  # scores stay small beside the scale
-        c.q *= np.float32(2.0 ** -100)
+        c.kv_scale[..., :2] *= np.float32(2.0 ** 122)  # scores stay small beside the scale
+        c.q *= np.float32(2.0 ** -112)
         Call(qsa, c, t).check("K scales")
 
 
