@@ -197,7 +197,8 @@ qsa_status check_attn(const qsa_shape *s, int n_seq, int n_pools, int max_select
 {
     const qsa_status st = kv4_check(s, n_seq, n_pools);
     if (st != QSA_OK) return st;
-    if (n_seq < 1 || max_selected < 0 || s->q_per_kv < 1 || s->n_queries < 1 || !isfinite(s->softmax_scale))
+    if (n_seq < 1 || max_selected < 0 || s->q_per_kv < 1 || s->n_queries < 1 ||
+        !(fabsf(s->softmax_scale) < 0x1p100f)) // (nor NaN; the kernels take it times powers of two)
         return QSA_ERR_INVALID_ARG;
     if (s->q_dtype != QSA_F32 && s->q_dtype != QSA_BF16) return QSA_ERR_INVALID_ARG;
     if (n_seq > 65535 || s->q_per_kv > 64 || s->n_queries > 65536 || max_selected > 0x7fffffff - 1024 ||

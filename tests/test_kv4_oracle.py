@@ -264,6 +264,16 @@ def test_attn_shape_refused(lib, field, value, code):
         assert lib.qsa_kv4_attn_workspace_bytes(ctypes.byref(s), 3, 100, ctypes.byref(ctypes.c_size_t(0))) == code
 
 
+@pytest.mark.parametrize("value,ok", [(2.0 ** 100, False), (-2.0 ** 127, False), (3e38, False), (2.0 ** 99, True), (0.0, True)])
+def test_attn_softmax_scale_refused(lib, value, ok):
+    """Scales that the kernels' scaling by powers of two would overflow."""
+    bytes_ = ctypes.c_size_t(0)
+    s = shape(softmax_scale=value)
+    assert lib.qsa_kv4_attn_workspace_bytes(ctypes.byref(s), 3, 100, ctypes.byref(bytes_)) == (qsa.QSA_OK if ok else INVALID)
+    if not ok:
+        assert attn_call(lib, s) == INVALID
+
+
 def test_attn_workspace_bytes(lib):
     size = qsa.qsa_kv4_attn_workspace_bytes(shape(), 3, 100)
     assert size > 0 and size % 256 == 0
