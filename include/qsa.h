@@ -446,8 +446,10 @@ qsa_status qsa_kv4_read(const qsa_shape *shape, int32_t n_seq, int32_t n_pools, 
  * query holds one, are not finite, and no other row is.  Two
  * launches; allocates nothing, graph-capturable.  Errors: QSA_ERR_INVALID_ARG;
  * QSA_ERR_UNSUPPORTED (head_dim != 256, q_per_kv above 64, n_queries above
- * 65536, n_seq above 65535, max_selected within 1024 of 2^31, or 2^31 or more
- * query rows); QSA_ERR_WORKSPACE; QSA_ERR_CUDA.
+ * 65536, n_seq above 65535, max_selected within 1024 of 2^31, 2^31 or more query
+ * rows, 2^32 - 1 or more (pool, KV head, cell) rows in all, which the append and
+ * the read accept, or 2^31 or more tiles of 128 cells for each multiprocessor);
+ * QSA_ERR_WORKSPACE; QSA_ERR_CUDA.
  */
 qsa_status qsa_kv4_attn_workspace_bytes(const qsa_shape *shape, int32_t n_seq,
                                         int32_t max_selected, size_t *bytes);

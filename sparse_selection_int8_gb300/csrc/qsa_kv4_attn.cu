@@ -245,6 +245,8 @@ extern "C" qsa_status qsa_kv4_attn_batch(const qsa_shape *shape, int32_t n_seq, 
     for (const void *a : {(const void *)q, (const void *)kv_pool, (const void *)kv_scale})
         if (out == a || (workspace && workspace == a) || out == workspace) return QSA_ERR_INVALID_ARG;
     if (workspace_bytes < d.total) return QSA_ERR_WORKSPACE;
+    // (rows of the pools are numbered in 32 bits)
+    if ((long long)n_pools * shape->n_kv_heads > 0xfffffffell / shape->pool_cells) return QSA_ERR_UNSUPPORTED;
 
     AttnParams p{};
     p.pool = kv4_pool(shape, n_pools, page_table);
@@ -288,8 +290,7 @@ extern "C" qsa_status qsa_kv4_attn_batch(const qsa_shape *shape, int32_t n_seq, 
     // (measured: a second segment costs the kernel for wide windows 14 us, 7 tiles;
     // the other one's batched decode takes 22.3 us without this, 18.1 with)
     p.seg_tiles = d.slot_rows == kWideRows ? 7 : 1;
-    if (tiles / cap >= 0x7fffffffll || (long long)n_pools * shape->n_kv_heads > 0xfffffffell / shape->pool_cells)
-        return QSA_ERR_UNSUPPORTED;
+    if (tiles / cap >= 0x7fffffffll) return QSA_ERR_UNSUPPORTED;
     const int grid = (int)(tiles < 1 ? 1 : tiles < cap ? tiles : cap);
     const cudaError_t e = d.slot_rows == kWideRows ? launch_wide(p, grid, cs)
                           : d.parts == 1 ? launch_single(p, d.rb_rows, grid, cs) : launch_split(p, d.rb_rows, grid, cs);

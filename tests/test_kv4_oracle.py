@@ -274,6 +274,12 @@ def test_attn_softmax_scale_refused(lib, value, ok):
         assert attn_call(lib, s) == INVALID
 
 
+def test_attn_pools_of_2_to_32_rows_refused(lib):
+    """Refused by the host's checks, before the device is asked anything."""
+    assert attn_call(lib, shape(n_kv_heads=65535, pool_cells=1 << 16, page_table_len=4096), n_seq=2, n_pools=2) == UNSUPPORTED
+    assert attn_call(lib, shape(n_kv_heads=1, pool_cells=1 << 30, page_table_len=1 << 20), n_seq=4, n_pools=4) == UNSUPPORTED
+
+
 def test_attn_workspace_bytes(lib):
     size = qsa.qsa_kv4_attn_workspace_bytes(shape(), 3, 100)
     assert size > 0 and size % 256 == 0
