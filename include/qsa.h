@@ -31,12 +31,19 @@
  *   - Kernels are launched with programmatic dependent launch: a call's first
  *     kernel may start while the previous kernel on the stream is still
  *     running, if that kernel allows it (a kernel that calls
- *     cudaTriggerProgrammaticLaunchCompletion, as this library's do).  Until
- *     it has waited for that kernel, a call only reads its own inputs
- *     (queries, pools, scales, page table, list, offsets) and writes nothing
- *     but status bits; so a kernel that triggers early must not write the
- *     next call's inputs after its trigger.  Copies, events and ordinary
- *     launches before a call are complete before it starts.  The next kernel
+ *     cudaTriggerProgrammaticLaunchCompletion, as this library's do) or once
+ *     all its blocks have ended.  The calls on 4-bit cells and qsa_page_map
+ *     wait for that kernel before they read anything.  The attention calls on
+ *     INT8 pools (qsa_decode_attn_*) do not: until they have waited they read
+ *     their own inputs (queries, pools, scales, page table, list, offsets,
+ *     limits) and write nothing but status bits.  So a kernel that triggers
+ *     early must not write such a call's inputs after its trigger; and since
+ *     CUDA promises a kernel's writes to a launch that may start early only
+ *     behind that launch's wait, a kernel that writes them directly before
+ *     such a call has to fence its last writes (__threadfence(), as this
+ *     library's kernels do), or another ordinary launch or a copy has to
+ *     stand between the two.  Copies, and whatever lies before an ordinary
+ *     launch or a copy, are complete before a call starts.  The next kernel
  *     on the stream may start early too: a kernel launched after a call with
  *     the programmatic-serialization attribute must call
  *     cudaGridDependencySynchronize() before it reads the call's outputs (the

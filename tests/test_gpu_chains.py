@@ -88,6 +88,27 @@ def test_attention_behind_the_int8_append(qsa, n_seq, G):
     assert int(d.status.item()) == 0
 
 
+@pytest.mark.parametrize("n_seq,G", [(1, 1), (4, 2)])
+def test_int8_attention_behind_ordinary_kernels(qsa, n_seq, G):
+    """Each input in turn written by a framework's kernel, another ordinary kernel between it and the call."""
+    sets = [qsa.DeviceProblem(wl.make_problem(n_seq=n_seq, n_kv_heads=G, n_queries=2, pool_cells=2048, n_selected=[900] * n_seq,
+                                              chunk_cells=128, seed=9840 + i)) for i in range(2)]
+    d = qsa.DeviceProblem(sets[0].p)
+    names = ["sel", "sel_offsets", "page_table", "q", "k_scale", "v_scale", "k_pool", "v_pool"]
+    other = torch.zeros(1, device="cuda")
+    for last in range(len(names)):
+        def step(i, wait):
+            for n in names[last + 1:] + names[:last + 1]:
+                torch.add(getattr(sets[i], n), 0, out=getattr(d, n))
+            other.add_(1)
+            wait()
+            out = torch.empty((n_seq, 2, G * 12, 256), device="cuda")
+            qsa.qsa_decode_attn_batch(d.shape, n_seq, d.q, d.k_pool, d.v_pool, d.k_scale, d.v_scale, d.page_table, d.sel,
+                                      d.sel_offsets, 900, out, d.workspace, d.ws_bytes, d.status)
+            return out
+        run_twice(step, 2, 5)
+
+
 @pytest.mark.parametrize("T", [4, 700])  # the maps by one launch, by two
 def test_limited_attention_behind_the_page_map(qsa, T):
     """INT8 pools whose tables, offsets and limits are the page map's: a window of T tokens that comes and goes."""
