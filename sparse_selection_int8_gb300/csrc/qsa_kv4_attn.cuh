@@ -811,6 +811,9 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_kv4_attn_kernel(const AttnPar
                 // limits between the rows: row by row
                 const bool by_row = lim_min < 0 || __any_sync(0xffffffffu, !none && pos >= lim_min);
                 f.w = fmaf(7.5f, f.z, f.w); // (V's codes go in less 7.5)
+                // with care where an unseen cell's V scale (as P' takes it) or zero is not
+                // finite: a row's sigma may be far below a scale that it does not see
+                const bool care = by_row && __any_sync(0xffffffffu, !(fabsf(f.z) * ms.isg_max[set] < INFINITY && fabsf(f.w) < INFINITY));
                 const float avs = none ? 0.f : fmaxf(fabsf(f.z), 0x1p-98f);
                 const float2 ks = make_float2(f.x, f.x), kz = make_float2(f.y, f.y), vs = make_float2(f.z, f.z),
                              vz = make_float2(f.w, f.w);
@@ -970,12 +973,10 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_kv4_attn_kernel(const AttnPar
                         const float2 pe2 = make_float2(fast_exp2(x[r].x), fast_exp2(x[r].y));
                         float2 pv;
                         l[r] = add2(l[r], pe2);
-                        if (!by_row) {
+                        if (!care) {
                             z[r] = fma2(pe2, vz, z[r]);
                             pv = mul2(pe2, mul2(vs, isg));
-                        } else {
-                            // what an unseen cell holds must not reach the row: not finite, or
-                            // finite but beyond the row's sigma, which may be far below it
+                        } else { // (what an unseen cell holds must not reach the row)
                             float2 &zr = z[r];
                             pv.x = x[r].x != -INFINITY ? pe2.x * (f.z * isg.x) : 0.f;
                             pv.y = x[r].y != -INFINITY ? pe2.y * (f.z * isg.y) : 0.f;
