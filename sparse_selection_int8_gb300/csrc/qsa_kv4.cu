@@ -12,9 +12,9 @@
 // one 16- or 32-byte load per lane and its codes one 4-byte word per lane (128
 // contiguous bytes per warp store), and minimum and maximum are two warp
 // reductions.  65,536 (cell, KV head) rows: append of fp32 25.6 us (5.9 TB/s), of
-// bf16 19.5 us (4.4 TB/s; bound by its instructions, a third of them for quotients
+// bf16 20.2 us (4.2 TB/s; bound by its instructions, a third of them for quotients
 // on a border between codes, which bf16 values often give); read to fp32 29 us (5.2
-// TB/s, writes mostly), to bf16 12.9 us (6.6 TB/s).
+// TB/s, writes mostly), to bf16 16.9 us (5.0 TB/s; 12.9 where the output fits the L2).
 #include "qsa_kv4.cuh"
 #include "qsa_sm100.cuh"
 

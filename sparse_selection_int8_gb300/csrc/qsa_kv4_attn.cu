@@ -30,12 +30,18 @@
 // by a power of two sigma not below the largest so far, so that P' = p vs / sigma
 // stays inside f16.  p, sums, maxima and outputs are fp32.
 //
-// What bounds it, by ncu: whole contexts (8 rows a KV head, 900,000 cells, 63 us
-// for 245 MB: 3.9 TB/s) the shared memory, 80% busy with a tile's 32 KB of codes in
-// and out, 64 KB of expanded V codes in and out and P'; long selections in fp32 (24
-// rows, 35 us for 71 MB) that and the softmax; calls of a few tiles latency: a
-// chain of list, page, cells, expansion, softmax, P V and merge, 6 us.  A plain
-// gather of the cells takes 43 and 15 us.
+// What bounds it, by ncu: whole contexts (8 rows a KV head, 900,000 cells, 65 us
+// for 245 MB: 3.8 TB/s) keep the shared memory 88% busy with a tile's 32 KB of codes
+// in and out, 64 KB of expanded V codes in and out and P' (whether that or the
+// softmax's latency is the limit is not settled: halving V's share with 8-bit operands
+// changed little); long selections in fp32 (24 rows, 38 us for 71 MB) that and the
+// softmax; calls of a few tiles latency: a chain of list, page, cells, expansion,
+// softmax, P V and merge, 9 us.  A plain gather of the cells takes 43 and 15 us.
+//
+// Every input is read behind the wait for the kernel before.  Lists, tables and
+// cells read ahead of it would take 2.4 to 2.9 us off each call in a row (6.3 us for one
+// of a few tiles), but CUDA promises them only behind it.  The figures of single
+// choices, here and in the other files, are from before that: both sides lack it.
 //
 // Tried and slower: mma.sync (68 us whole, 64 long; its 8-bit float forms are
 // carried out in f16), tcgen05 with e4m3 operands (65 us whole, but 31 against 25

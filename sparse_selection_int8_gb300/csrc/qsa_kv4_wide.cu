@@ -16,7 +16,7 @@
 // A tile takes 2.1 us, twice what the tensor cores need: 3.8 K cycles of shared
 // memory, of which the operands' reads (192 KB) are 1.5 K, the expanded codes'
 // stores 1 K and the softmax's reads of scales and zeros most of the rest (ncu),
-// behind the softmax's own latency.  3,084 rows of two heads over 8,000 cells: 63 us
+// behind the softmax's own latency.  3,084 rows of two heads over 8,000 cells: 64 us
 // (50.5 GFLOP, 41% of the measured tensor rate), where blocks of 32 rows take 137.
 // A softmax thread per half row, which reads four times as many scales, took 68.
 #include "qsa_kv4_attn.cuh"

@@ -673,6 +673,76 @@ def test_attend_long_sums(qsa, H, t):
     assert (err / norm) ** 0.5 <= (3e-6 if t == "f32" else 2.0 ** -8)
 
 
+@pytest.mark.parametrize("kw,t", [(dict(n_seq=3, G=2, lens=(600, 0, 77)), "f32"), (dict(n_seq=2, H=12, T=8, lens=(900, 5)), "bf16"),
+                                  (dict(n_seq=40, lens=(300, 2), T=2), "f32")], ids=str)
+def test_attend_short_lists_under_the_largest_bound(qsa, kw, t):
+    """max_selected at its limit (and so the work list in 64 bits): short lists as ever."""
+    c = Attend(seed=82, q_dtype=t, **kw)
+    c.max_selected = 2 ** 31 - 1 - 1024
+    Call(qsa, c, t).check()
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_attend_as_many_sequences_as_there_can_be(qsa, t):
+    """65,535 contexts of no or one cell: zeros, or that cell's values."""
+    B = 65535
+    dt, code = (torch.float32, qsa.QSA_F32) if t == "f32" else (torch.bfloat16, qsa.QSA_BF16)
+    g = torch.Generator(device="cuda").manual_seed(83)
+    pool = torch.randint(0, 256, (1, 1, B, 256), generator=g, dtype=torch.uint8, device="cuda")
+    scale = torch.rand(1, 1, B, 4, generator=g, device="cuda") + 0.1
+    q = torch.randn(B, 1, 3, 256, generator=g, device="cuda").to(dt)
+    table = torch.randperm(B, generator=g, device="cuda").int()[:, None].contiguous()
+    one = torch.rand(B, generator=g, device="cuda") < 0.7
+    offsets = torch.cat([torch.zeros(1, device="cuda"), one.cumsum(0)]).int()
+    shape = qsa.make_shape(n_kv_heads=1, q_per_kv=3, n_queries=1, pool_cells=B, page_table_len=1, chunk_cells=1, softmax_scale=1 / 16,
+                           q_dtype=code)
+    ws = torch.empty(qsa.qsa_kv4_attn_workspace_bytes(shape, B, 1), dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, 3.0)
+    qsa.qsa_kv4_attn_batch(shape, B, 1, q, pool, scale, table, None, offsets, 1, None, code, out, ws, ws.numel())
+    f = scale[0, 0, table[:, 0].long()].double()
+    v = pool[0, 0, table[:, 0].long(), 128:]
+    want = torch.stack([v & 15, v >> 4], -1).flatten(-2).double() * f[:, 2:3] + f[:, 3:4]
+    assert not out[~one].any()
+    # one weight of 1: P' (2^-22, or 2^-11 of a code's part) and the output's rounding
+    err = (out[one].double() - want[one][:, None, None]).abs()
+    part = (7.5 * f[one][:, 2:3])[:, None, None]
+    eps = 2.0 ** -20 * (want[one][:, None, None].abs() + part) if t == "f32" else 2.0 ** -11 * part + 2.0 ** -8 * (want[one][:, None, None] + part * 2.0 ** -11)
+    assert bool((err <= eps + 2.0 ** -20 * part).all())
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_attend_widest_window(qsa, t):
+    """65,536 queries of 64 heads: 2^22 rows, their offsets past 2^31 bytes, over five cells with limits of their own."""
+    H, T, n = 64, 65536, 5
+    dt, code = (torch.float32, qsa.QSA_F32) if t == "f32" else (torch.bfloat16, qsa.QSA_BF16)
+    g = torch.Generator(device="cuda").manual_seed(84)
+    pool = torch.randint(0, 256, (1, 1, n, 256), generator=g, dtype=torch.uint8, device="cuda")
+    r = torch.rand(1, 1, n, 4, generator=g, device="cuda")
+    scale = torch.empty_like(r)
+    scale[..., 0::2] = 0.05 + 0.3 * r[..., 0::2]
+    scale[..., 1::2] = -7.5 * scale[..., 0::2] + r[..., 1::2] - 0.5
+    q = torch.randn(1, T, H, 256, generator=g, device="cuda").to(dt)
+    limit = torch.randint(0, n + 1, (1, T), generator=g, device="cuda").int()
+    table = torch.arange(n, device="cuda").int()[None].contiguous()
+    shape = qsa.make_shape(n_kv_heads=1, q_per_kv=H, n_queries=T, pool_cells=n, page_table_len=n, chunk_cells=1, softmax_scale=1 / 16,
+                           q_dtype=code)
+    ws = torch.empty(qsa.qsa_kv4_attn_workspace_bytes(shape, 1, n), dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, 3.0)
+    qsa.qsa_kv4_attn_batch(shape, 1, 1, q, pool, scale, table, None, dev(np.array([0, n], np.int32)), n, limit, code, out, ws, ws.numel())
+    u = torch.stack([pool[0, 0] & 15, pool[0, 0] >> 4], -1).flatten(-2).double()
+    f = scale[0, 0].double()
+    k, v = u[:, :256] * f[:, 0:1] + f[:, 1:2], u[:, 256:] * f[:, 2:3] + f[:, 3:4]
+    for t0 in range(0, T, 4096):
+        x = q[0, t0:t0 + 4096].double() @ k.T / 16
+        seen = torch.arange(n, device="cuda") < limit[0, t0:t0 + 4096, None, None]
+        w = torch.where(seen, (x - x.masked_fill(~seen, -1e300).amax(-1, keepdim=True)).exp(), torch.zeros_like(x))
+        ref = torch.nan_to_num(w / w.sum(-1, keepdim=True)) @ v
+        got = out[0, t0:t0 + 4096].double()
+        assert not got[limit[0, t0:t0 + 4096] == 0].any()
+        err = (got - ref).norm(dim=-1) / ref.norm(dim=-1).clamp_min(1e-30)  # by row: no row in another's place
+        assert float(err.max()) <= (2e-5 if t == "f32" else 2.0 ** -8), t0
+
+
 def test_attend_cells_past_32_bit_offsets(qsa):
     """Slots whose rows lie past 2^32 bytes of the pool."""
     cells = 18_000_000
