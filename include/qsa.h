@@ -444,7 +444,8 @@ qsa_status qsa_kv4_read(const qsa_shape *shape, int32_t n_seq, int32_t n_pools, 
  * magnitude (a larger scale is refused), the values of a list's cells times
  * their number below 2^126.  Scores and sums are fp32; into the tensor cores go the codes exactly,
  * queries to 2^-22 of their value (bf16 ones exactly) or 2^-35 of their row's
- * largest, probabilities to 2^-22 (2^-11 where queries and output are bf16).
+ * largest, probabilities times V scales to 2^-22 (2^-11 where queries and output
+ * are bf16) or 2^-30 of the largest V scale that the row sees.
  * Unlike the other attention calls this one waits for the kernel before it, if
  * that let it start early, before it reads any input: whatever that kernel
  * writes may be one, and the output of one call may be the query of the next.

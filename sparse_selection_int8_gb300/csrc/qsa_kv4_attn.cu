@@ -31,7 +31,7 @@
 // stays inside f16.  p, sums, maxima and outputs are fp32.
 //
 // What bounds it, by ncu: whole contexts (8 rows a KV head, 900,000 cells, 65 us
-// for 245 MB: 3.8 TB/s) keep the shared memory 88% busy with a tile's 32 KB of codes
+// for 245 MB: 3.8 TB/s) keep the shared memory 87% busy with a tile's 32 KB of codes
 // in and out, 64 KB of expanded V codes in and out and P' (whether that or the
 // softmax's latency is the limit is not settled: halving V's share with 8-bit operands
 // changed little); long selections in fp32 (24 rows, 38 us for 71 MB) that and the
