@@ -442,15 +442,16 @@ qsa_status qsa_kv4_read(const qsa_shape *shape, int32_t n_seq, int32_t n_pools, 
  *              whose kernels may overlap need one each.
  * softmax_scale and its products with the queries' values stay below 2^100 in
  * magnitude (a larger scale is refused), the values of a list's cells times
- * their number below 2^126.  Scores and sums are fp32; into the tensor cores go the codes exactly,
- * queries to 2^-22 of their value (bf16 ones exactly) or 2^-35 of their row's
- * largest, probabilities times V scales to 2^-22 (2^-11 where queries and output
+ * their number below 2^126.
+ * Scores and sums are fp32; into the tensor cores go the codes exactly, queries
+ * to 2^-22 of their value (bf16 ones exactly) or 2^-35 of their row's largest,
+ * probabilities times V scales to 2^-22 (2^-11 where queries and output
  * are bf16) or 2^-30 of the largest V scale that the row sees.
  * Unlike the other attention calls this one waits for the kernel before it, if
  * that let it start early, before it reads any input: whatever that kernel
  * writes may be one, and the output of one call may be the query of the next.
- * (So do qsa_kv4_append, qsa_kv4_read and qsa_page_map.)  Cells that a row does not see do not reach it, whatever
- * their stored values; rows that do see a value that is not finite, or whose
+ * (So do qsa_kv4_append, qsa_kv4_read and qsa_page_map.)
+ * Cells that a row does not see do not reach it, whatever their stored values; rows that do see a value that is not finite, or whose
  * query holds one, are not finite, and no other row is.  Two
  * launches; allocates nothing, graph-capturable.  Errors: QSA_ERR_INVALID_ARG;
  * QSA_ERR_UNSUPPORTED (head_dim != 256, q_per_kv above 64, n_queries above

@@ -39,7 +39,7 @@
 // softmax, P V and merge, 9 us.  A plain gather of the cells takes 43 and 15 us.
 //
 // Every input is read behind the wait for the kernel before.  Lists, tables and
-// cells read ahead of it would take 2.4 to 2.9 us off each call in a row (6.3 us for one
+// cells read ahead of it would take 2.5 to 3.1 us off each call in a row (6.3 us for one
 // of a few tiles), but CUDA promises them only behind it.  The figures of single
 // choices, here and in the other files, are from before that: both sides lack it.
 //

@@ -526,15 +526,16 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_kv4_attn_kernel(const AttnPar
     }
     // rows of the pool from the start: a wait that runs out lets the copies read them early
     for (int i = tid; i < kRow * kTile; i += kThreads) (&ms.row[0][0])[i] = 0u;
+    // All input is read behind this: the kernel before may have written any of it (the
+    // merge of a call whose output is this one's query, a copy into a list or a page
+    // table), and its writes are promised here only; it may also still read the
+    // partials that this one writes.  Tensor memory is taken behind it too: a kernel
+    // that let this one start may yet need it to end.
+    cudaGridDependencySynchronize();
     if (w == kSWarp) {
         tmem_alloc(&ms.tmem, kTmemCols);
         tmem_relinquish();
     }
-    // All input is read behind this: the kernel before may have written any of it (the
-    // merge of a call whose output is this one's query, a copy into a list or a page
-    // table), and its writes are promised here only; it may also still read the
-    // partials that this one writes.
-    cudaGridDependencySynchronize();
     if (w == kSoft0) {
         Walk f;
         long long t;

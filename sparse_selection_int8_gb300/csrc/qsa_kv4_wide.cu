@@ -96,12 +96,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) qsa_kv4_wide_kernel(const Att
     }
     // rows of the pool from the start: a wait that runs out lets the loads read them early
     for (int i = tid; i < kWRow * kTile; i += kWideThreads) (&ms.row[0][0])[i] = 0u;
+    // All input is read, and tensor memory taken, behind this (see qsa_kv4_attn_kernel).
+    cudaGridDependencySynchronize();
     if (w == kWMma) {
         tmem_alloc(&ms.tmem, 512);
         tmem_relinquish();
     }
-    // All input is read behind this (see qsa_kv4_attn_kernel).
-    cudaGridDependencySynchronize();
     if (w == 0) {
         Walk f;
         long long t;
