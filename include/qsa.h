@@ -441,8 +441,8 @@ qsa_status qsa_kv4_read(const qsa_shape *shape, int32_t n_seq, int32_t n_pools, 
  *              bytes, 256-byte aligned, no initialisation needed; two calls
  *              whose kernels may overlap need one each.
  * softmax_scale and its products with the queries' values stay below 2^100 in
- * magnitude (a larger scale is refused), the values of a list's cells times
- * their number below 2^126.
+ * magnitude (a larger scale is refused); the scores, and the values of a list's
+ * cells times their number, below 2^126.
  * Scores and sums are fp32; into the tensor cores go the codes exactly, queries
  * to 2^-22 of their value (bf16 ones exactly) or 2^-35 of their row's largest,
  * probabilities times V scales to 2^-22 (2^-11 where queries and output
